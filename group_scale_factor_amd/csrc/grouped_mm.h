@@ -683,7 +683,7 @@ __global__ __launch_bounds__(TW *NW *kWave) void mm_tile_kernel(MmParams p) {
 // the group's rows), "multiply" replaces each as soon as its products are issued.
 //
 // A load may go to a place one slot after the place was last read, and has to be there a slot before the next read:
-//   w                    last read in slot 2s+1 (others); the next, s+2's, in slot 2s+4 (lead)
+//   w, its scales        last read in slot 2s+1 (others); the next, s+2's, in slot 2s+4 (lead)
 //   t, lead              last read in slots 2s, 2s+1; next 2s+4, 2s+5
 //   t, others            last read in slots 2s+1, 2s+2; next 2s+5, 2s+6
 // A load of 1 KB keeps a wave for 61 cycles where the four waves of a group issue theirs together (64 bytes a cycle
@@ -833,6 +833,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
   const uint32_t ws_read = ws_at + (MX ? scale_row_offset(w_lane, 1) : DEPTH ? w_lane * 4 : n_first / kTileRows * 4);
   v8i w[4], t[4];
   uint32_t ts[MX ? TF : 4], ws[MX || DEPTH ? 4 : 1];
+  uint32_t wf[DEPTH && !MX ? 16 : 1];      // block-128 scales of the outputs that the lane has, to multiply with
   const auto read_t = [&](int st, int i) {
     const uint8_t *from = mm_lds + st * S::Stage + i * 16 * kStep;
     t[i & 3] = operand(*reinterpret_cast<const uint4 *>(from + t_read),
@@ -849,9 +850,13 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
   uint32_t seen;              // block-128 scale that the lane looks at, its row
   const int seen_row = nw < 2 ? t_first + nw * 64 + lane : (tw * 2 + nw - 2) * 64 + lane;
   int first_other;            // step
-  const auto read_scales = [&](int st) {
+  const auto read_scales = [&](int st, auto SCALED) {
     const uint8_t *scales = mm_lds + st * S::ScaleStage;
-    if (MX) {
+    if (DEPTH && !MX && !SCALED) {
+#pragma unroll
+      for (int n = 0; n < int(sizeof(wf) / 4); ++n)
+        wf[n] = *reinterpret_cast<const uint32_t *>(scales + ws_at + (n_first + g * 8 + n / 8 * 32 + n % 8) * 4);
+    } else if (MX) {
       // rows r, r+32, .. of a 128-row block share 16 bytes, rows r+16, .. the ones 256 bytes on
 #pragma unroll
       for (int h = 0; h < 2; ++h) ts_words[h] = *reinterpret_cast<const uint4 *>(scales + ts_read + h * 256);
@@ -912,12 +917,6 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
     pin();
   };
   const auto multiply_any = [&](int st) __attribute__((always_inline)) {
-    uint32_t wf[DEPTH ? 16 : 1];      // of the outputs that the lane has
-#pragma unroll
-    for (int n = 0; n < int(sizeof(wf) / 4); ++n)
-      wf[n] = DEPTH ? *reinterpret_cast<const uint32_t *>(mm_lds + st * S::ScaleStage + ws_at +
-                                                          (n_first + g * 8 + n / 8 * 32 + n % 8) * 4)
-                    : ws[0];
     constexpr int kBehind = 4;        // one product, then the sums of the one so many behind: five parts live
     v4f part[kBehind + 1];
     float factor[2];
@@ -926,12 +925,12 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         acc[i][n][e] = fmaf(part[at % (kBehind + 1)][e],
-                            DEPTH ? factor[i & 1] * __uint_as_float(wf[DEPTH ? n * 4 + e : 0]) : factor[i & 1],
+                            DEPTH ? factor[i & 1] * __uint_as_float(wf[DEPTH && !MX ? n * 4 + e : 0]) : factor[i & 1],
                             acc[i][n][e]);
     };
 #pragma unroll
     for (int i = 0; i < TF; ++i) {
-      factor[i & 1] = __uint_as_float(ts[i & 3]) * (DEPTH ? 1.0f : __uint_as_float(wf[0]));
+      factor[i & 1] = __uint_as_float(ts[i & 3]) * (DEPTH ? 1.0f : __uint_as_float(ws[0]));
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int at = i * 4 + n;
@@ -1014,7 +1013,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
             read_w(st, n);
             load_w(ls, to, n);
           }
-          read_scales(st);
+          read_scales(st, SCALED);
           load_w(ls, to, 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1033,7 +1032,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
 #pragma unroll
           for (int n = 0; n < 4; ++n) read_w(st, n);
           load_t(ls, to, 0, 0);
-          read_scales(st);
+          read_scales(st, SCALED);
           load_t(ls, to, 0, 1);
           read_t(st, 0);
           load_t_scales(ls, to);
