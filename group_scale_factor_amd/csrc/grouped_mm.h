@@ -966,7 +966,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
 
     // The step after a tile's last is the next tile's first: its loads take the same slots.
     int s = 0, st = 0;        // step to multiply, its stage
-    int all = max(steps, 1);  // of the tile; one of no steps is one of zeros
+    int all = steps;          // of the tile; one of none is a step of zeros
     bool more = true, whole = false;      // whole: all of the stores of the tile before are on the count of loads
     int done = 0;             // steps of all tiles
     uint32_t this_block = block - gridDim.x, last_block = this_block;
@@ -996,7 +996,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
       clear();
       out = j.out, out_t = j.t_rows, out_w = j.w_rows;
       last_block = this_block, this_block = block - gridDim.x;
-      s = 0, all = max(steps, 1);
+      s = 0, all = steps;
       return more;
     };
     // Loads that may be under way at the end of a slot, the newest ones. lead: the second half's 2, whose use is two
@@ -1046,9 +1046,11 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
         if (kChecked && SCALED) {
           // The eight waves look at 64 of a step's scales each, and what one finds ends all waves' next step: by then
           // it is written. (The lead's finds of that next step may be there, too.) 1 .. 254: a power of two in the
-          // normal range. Rows past the tile's last have codes 0.
+          // normal range. Rows past the tile's last have codes 0, and so has a tile of no steps (a group of no tokens),
+          // whose scales are zeros that no cast wrote.
           if (__builtin_amdgcn_readfirstlane(first_other) < done) break;
-          const bool power = __builtin_rotateright32(seen, 23) - 1 < 254 || seen_row >= (nw < 2 ? out_t : out_w);
+          const bool power =
+              __builtin_rotateright32(seen, 23) - 1 < 254 || seen_row >= (nw < 2 ? out_t : out_w) || all == 0;
           if (__ballot(!power) != 0) {
             if (lane == 0) atomicMin(other, done);
             reads_written();

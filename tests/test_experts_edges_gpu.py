@@ -1,0 +1,34 @@
+"""Calls at the edges of the expert layer's operators: what no group or row of them may notice (GPU)."""
+
+import numpy as np
+import pytest
+import torch
+
+import group_scale_factor_amd as gsf
+from test_experts_products_gpu import DEV, ends_of, random_codes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("empty", [[1], [0, 7], [2, 3, 4]])
+def test_empty_token_groups_leave_the_others_bits(empty):
+    """Scales that are powers of two: with a group of no tokens or without it, the other groups' sums take the same
+    instructions. More large tiles than compute units, so that a workgroup goes on from an empty group's tile."""
+    sizes, M, N = [500, 700, 1, 128, 256, 384] * 2, 1272, 1528
+    with_empty = list(sizes)
+    for g in empty:
+        with_empty.insert(g, 0)
+    T = sum(sizes)
+    gen = torch.Generator(device=DEV).manual_seed(len(empty))
+    Tp = gsf.fp8_quantize_cols_K_groups_tokens(T, len(with_empty))
+    codes = [random_codes(gen, n, Tp) for n in (M, N)]
+    scales = [torch.exp2(torch.randint(-12, 12, (Tp // 128, n), generator=gen, device=DEV).double()).float()
+              for n in (M, N)]
+    res = []
+    for these in (sizes, with_empty):
+        tp = gsf.fp8_quantize_cols_K_groups_tokens(T, len(these))
+        (a, b), (asc, bsc) = [c[:, :tp].contiguous() for c in codes], [s[: tp // 128].contiguous() for s in scales]
+        res.append(gsf.fp8_grouped_mm_K_groups(a, asc, b, bsc, ends_of(these)))
+    kept = torch.tensor([n > 0 for n in with_empty], device=DEV)
+    assert torch.equal(res[1][kept], res[0])
+    assert bool((res[1][~kept] == 0).all())
