@@ -7,10 +7,10 @@
 // find each other with one ballot per bucket bit (the AND over the bits of the
 // ballot or its complement), so a lane's place among them is a popcount and
 // the lowest one moves the bucket's counter: no atomics, the same plan on
-// every run. Up to 16384 slots (and 2048 experts) one workgroup does it all in one
-// launch: counts per wave, a scan over waves and buckets in LDS, placement. Beyond,
-// counts per run of 1024 slots, a scan along the runs of each bucket (from 65 runs
-// on; fewer are added up by the next kernel), placement.
+// every run. Up to 16384 slots (and 2048 experts, or no slots) one workgroup does it
+// all in one launch: counts per wave, a scan over waves and buckets in LDS,
+// placement. Beyond, counts per run of 1024 slots, a scan along the runs of each
+// bucket (from 65 runs on; fewer are added up by the next kernel), placement.
 //
 // The moves are HBM-bound copies. They go token by token, not sorted row by
 // row: a token's row is read once and written to its k places, and its k

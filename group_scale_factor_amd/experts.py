@@ -83,11 +83,11 @@ def experts_library():
 # compiles the headers and checks both.
 
 def moe_sort_tokens_workspace_bytes(tokens, topk, num_experts):
-    """4 * (E + 1) * (runs of 1024 slots + 1); 0 up to 16384 slots and 2048 experts; -1 for invalid sizes
-    (include/moe/moe_tokens.h)."""
+    """4 * (E + 1) * (runs of 1024 slots + 1); 0 up to 16384 slots and 2048 experts, and for no tokens; -1 for
+    invalid sizes (include/moe/moe_tokens.h)."""
     if tokens < 0 or not 1 <= topk <= 64 or not 1 <= num_experts <= 4096 or tokens > (0x7fffffff - 4096) // topk:
         return -1
-    if tokens * topk <= 16384 and num_experts <= 2048:
+    if tokens == 0 or tokens * topk <= 16384 and num_experts <= 2048:
         return 0
     return 4 * (num_experts + 1) * ((tokens * topk + 1023) // 1024 + 1)
 

@@ -57,13 +57,14 @@ enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
 /*
  * Bytes of the workspace of moe_sort_tokens: one count for each expert (and one
  * for the dropped slots) and run of 1024 slots, and one total for each; 0 for up to
- * 16384 slots and 2048 experts, which one workgroup sorts alone. -1 for invalid sizes.
+ * 16384 slots and 2048 experts, which one workgroup sorts alone, and for no slots.
+ * -1 for invalid sizes.
  */
 static inline int64_t moe_sort_tokens_workspace_bytes(int64_t tokens, int32_t topk, int32_t num_experts) {
   if (tokens < 0 || topk < 1 || topk > 64 || num_experts < 1 || num_experts > 4096 ||
       tokens > ((int64_t)0x7fffffff - 4096) / topk)
     return -1;
-  if (tokens * topk <= 16384 && num_experts <= 2048) return 0;
+  if (tokens == 0 || (tokens * topk <= 16384 && num_experts <= 2048)) return 0;
   return 4 * ((int64_t)num_experts + 1) * ((tokens * topk + 1023) / 1024 + 1);
 }
 

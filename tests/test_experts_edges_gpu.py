@@ -32,3 +32,13 @@ def test_empty_token_groups_leave_the_others_bits(empty):
     kept = torch.tensor([n > 0 for n in with_empty], device=DEV)
     assert torch.equal(res[1][kept], res[0])
     assert bool((res[1][~kept] == 0).all())
+
+
+@pytest.mark.parametrize("k,E", [(1, 2049), (8, 4096), (64, 2048), (2, 3)])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_sort_of_no_tokens_writes_the_ends(k, E, dtype):
+    ends = torch.full((E,), 7, dtype=torch.int32, device=DEV)
+    order = torch.empty(0, dtype=torch.int32, device=DEV)
+    position = torch.empty((0, k), dtype=torch.int32, device=DEV)
+    got = gsf.moe_sort_tokens(torch.empty((0, k), dtype=dtype, device=DEV), E, out=(ends, order, position))
+    assert got[0] is ends and bool((ends == 0).all())
