@@ -146,7 +146,7 @@ def _check_rows(t, name, dtypes, dims=2):
     shape, stride = t.shape, t.stride()
     if stride[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError("%s must have unit column stride" % name)
-    return stride[-2] if shape[-2] > 1 else shape[-1]
+    return stride[-2] if shape[-2] > 1 and shape[-1] > 0 else shape[-1]     # no second row, or rows of nothing: as dense
 
 
 def _check_codes(t, name, dims):
@@ -318,7 +318,8 @@ def _mm_M(mx, a, a_scales, w, w_scales, offs, out, stream):
     out, out_stride = _rows_output(out, "out", rows, N, torch.bfloat16, dev, stream)
     fn = lib.mx_grouped_mm_M_groups if mx else lib.fp8_grouped_mm_M_groups
     _check(fn(_ptr(a), _ptr(a_scales), rows, K, a_stride, _ptr(w), _ptr(w_scales), N,
-              w.stride(0) if G > 1 else N * w_row, w_row, _ptr(offs), G, _ptr(out), out_stride, _handle(stream, dev)))
+              w.stride(0) if G > 1 and K > 0 else N * w_row, w_row, _ptr(offs), G, _ptr(out), out_stride,
+              _handle(stream, dev)))
     return out
 
 

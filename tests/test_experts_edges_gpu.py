@@ -42,3 +42,20 @@ def test_sort_of_no_tokens_writes_the_ends(k, E, dtype):
     position = torch.empty((0, k), dtype=torch.int32, device=DEV)
     got = gsf.moe_sort_tokens(torch.empty((0, k), dtype=dtype, device=DEV), E, out=(ends, order, position))
     assert got[0] is ends and bool((ends == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["mx", "fp8"])
+@pytest.mark.parametrize("sizes,tail,N", [([3, 0, 5], 2, 40), ([1], 0, 16), ([300], 0, 300)])
+def test_row_products_over_no_depth_are_zeros(kind, sizes, tail, N):
+    rows, E = sum(sizes) + tail, len(sizes)
+    a = torch.empty((rows, 0), dtype=torch.uint8, device=DEV)
+    w = torch.empty((E, N, 0), dtype=torch.uint8, device=DEV)
+    if kind == "mx":
+        asc = wsc = torch.empty(0, dtype=torch.uint8, device=DEV)
+    else:
+        asc = torch.empty((0, rows), device=DEV)
+        wsc = torch.empty((E, -(-N // 128), 0), device=DEV)
+    out = torch.full((rows, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    mm = gsf.mx_grouped_mm_M_groups if kind == "mx" else gsf.fp8_grouped_mm_M_groups
+    assert mm(a, asc, w, wsc, ends_of(sizes), out=out) is out
+    assert bool((out == 0).all())
