@@ -314,7 +314,8 @@ struct MoveParams {
 };
 
 // A token's positions and weights, slot j in lane j: one load each for all of them, then read lane by lane (as
-// scalar loads they are one latency behind another).
+// scalar loads they are one latency behind another). A lane whose columns lie past the row stays to hold its slot: what
+// a lane's register holds once it has left is not defined. load_piece and store_piece touch nothing for it (n <= 0).
 struct Slots {
   int pos;
   float weight;
@@ -340,7 +341,6 @@ __global__ __launch_bounds__(kMoveThreads) void gather_kernel(MoveParams p) {
   const int c = (int(blockIdx.x - t * uint32_t(p.chunks)) * kMoveThreads + int(threadIdx.x)) * Piece<T>::V;
   const int n = p.cols - c;
   const Slots s = load_slots(p, t);
-  if (n <= 0) return;
   const Piece<T> v = load_piece(static_cast<const T *>(p.src) + t * p.src_ld + c, n);
   const Piece<T> zero = {};
   for (int j = 0; j < p.topk; ++j) {
@@ -360,7 +360,6 @@ __global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveParams p) {
   const int c = (int(blockIdx.x - t * uint32_t(p.chunks)) * kMoveThreads + int(threadIdx.x)) * V;
   const int n = p.cols - c;
   const Slots s = load_slots(p, t);
-  if (n <= 0) return;
   float sum[V] = {};
   for (int j0 = 0; j0 < p.topk; j0 += kAhead) {
     Piece<T> v[kAhead];
@@ -407,7 +406,8 @@ __global__ __launch_bounds__(kMoveThreads) void combine_backward_kernel(MovePara
     int pos[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) pos[i] = j0 + i < p.topk ? s.at(j0 + i) : -1;
-    for (int c = int(threadIdx.x) * V; c < p.cols; c += kMoveThreads * V) {
+    for (int c0 = 0; c0 < p.cols; c0 += kMoveThreads * V) {
+      const int c = c0 + int(threadIdx.x) * V;
       const int n = p.cols - c;
       const Piece<T> g = load_piece(dout + c, n);
       Piece<T> y[kAhead];

@@ -8,6 +8,7 @@ import pytest
 from group_scale_factor_amd import _build
 
 PRODUCTS = {s.rsplit("/", 1)[1].split("_")[0]: s for s in _build.EXPERT_SOURCES if "grouped_mm" in s}
+TOKENS = [s for s in _build.EXPERT_SOURCES if s.endswith("moe_tokens.hip")][0]
 READ_BYTES = {"b32": 4, "b64": 8, "b96": 12, "b128": 16}
 
 
@@ -50,3 +51,49 @@ def test_multiplying_slots_of_paired_waves_read_no_weights(assembly, kind):
         for s in slots:
             assert sum("mfma" in line for line in s) == 32, name
             assert lds_bytes_read(s) == 4 * 32 + (0 if kind == "mx" else 4 * 4), name
+
+
+def narrowed_lane_reads(lines):
+    """(reads of a lane by number, those of them that run while a branch holds lanes back). A branch on a condition
+    of the lanes saves the mask to a register and narrows it; the mask is whole again when that register comes back."""
+    at = {line.split(":")[0]: i for i, line in enumerate(lines) if line.startswith(".LBB")}
+    held = [None] * len(lines)      # mask registers saved and not yet back, on any way there
+    work = [(0, frozenset())]
+    while work:
+        i, state = work.pop()
+        while i < len(lines):
+            if held[i] is not None and state <= held[i]:
+                break
+            state = held[i] = state | (held[i] or frozenset())
+            line = lines[i]
+            m = re.match(r"s_(and|andn2|or)_saveexec_b64 ([^,\s]+), (\S+)", line)
+            if m:       # "andn2": on to the other side of a branch, whose mask lies in the second register
+                state = (state - {m.group(3)} if m.group(1) != "and" else state) | {m.group(2)}
+            m = re.match(r"s_xor_b64 (s[^,\s]+), exec, (\S+)", line)
+            if m:       # the lanes of the other side
+                state = state - {m.group(2)} | {m.group(1)}
+            m = re.match(r"s_andn2_b64 exec, exec, (\S+)", line)
+            if m:
+                state = state | {m.group(1)}
+            m = re.match(r"s_or_b64 exec, exec, (\S+)", line)
+            if m:
+                state = state - {m.group(1)}
+            m = re.match(r"s_(c?branch\S*) (\.LBB\S+)", line)
+            if m:
+                work.append((at[m.group(2)], state))
+            if line.startswith(("s_branch", "s_endpgm")):
+                break
+            i += 1
+    reads = [i for i, line in enumerate(lines) if re.match(r"v_readlane_b32 s\d+, v\d+, s\d+", line)]
+    return reads, [i for i in reads if held[i]]
+
+
+def test_token_moves_read_slots_from_lanes_that_are_there():
+    """A token's positions and weights lie one to a lane: a lane past the row's columns may not have left, or be held
+    back, where they are read. (The gradient of the sum keeps masks in vector lanes, which this walk does not follow.)"""
+    text = _build.device_assembly(TOKENS)
+    found = {**kernels(text, "gather_kernel"), **kernels(text, "combine_kernel")}
+    assert len(found) == 6
+    for name, lines in found.items():
+        reads, narrowed = narrowed_lane_reads(lines)
+        assert reads and not narrowed, name
