@@ -55,14 +55,71 @@ def device_assembly(source):
             return f.read()
 
 
+# A scalar register that a vector instruction writes (v_readfirstlane, v_readlane, a comparison) may be read by a
+# vector memory instruction five wait states later at the earliest. The compiler sees to that for its own memory
+# instructions and does not look into an asm block's.
+SCALAR_WAIT_STATES = 5
+
+
+def _scalars(operand):
+    """Numbers of the scalar registers that an operand names."""
+    m = re.match(r"s(\d+)$|s\[(\d+):(\d+)\]$", operand)
+    if not m:
+        return set()
+    return {int(m.group(1))} if m.group(1) else set(range(int(m.group(2)), int(m.group(3)) + 1))
+
+
+def early_scalar_reads(assembly):
+    """(vector instruction, memory instruction) pairs of one source's assembly that stand too close."""
+    found = []
+    for body in re.findall(r"^_Z\w+:[^\n]*\n(.*?)^\.Lfunc_end", assembly, re.S | re.M):
+        lines = [line.split(";")[0].strip() for line in body.splitlines()]
+        lines = [line for line in lines if line and (not line.startswith(".") or line.startswith(".LBB"))]
+        ways_in = {}     # label -> the branches to it
+        for i, line in enumerate(lines):
+            m = re.match(r"s_c?branch\S* (\.LBB\w+)", line)
+            if m:
+                ways_in.setdefault(m.group(1), []).append(i)
+
+        def walk(i, states, wanted, load, seen):
+            # back from `load` over every way to it, as far as the wait states reach
+            while i >= 0 and states < SCALAR_WAIT_STATES and (i, states) not in seen:
+                seen.add((i, states))
+                line = lines[i]
+                if line.startswith(".LBB"):
+                    for branch in ways_in.get(line.split(":")[0], []):
+                        walk(branch, states, wanted, load, seen)
+                    if i > 0 and lines[i - 1].startswith(("s_branch", "s_endpgm", "s_setpc")):
+                        return       # nothing comes from above
+                else:
+                    name, _, operands = line.partition(" ")
+                    if name.startswith("v_") and _scalars(operands.split(",")[0].strip()) & wanted:
+                        found.append((line, load))
+                        return
+                    states += int(operands) + 1 if name == "s_nop" else 1
+                i -= 1
+
+        for i, line in enumerate(lines):
+            if line.startswith(("buffer_", "global_", "scratch_", "flat_")):
+                words = [w for op in line.split(None, 1)[1].split(",") for w in op.split()[:1]]
+                wanted = set().union(*map(_scalars, words))
+                if wanted:
+                    walk(i - 1, 0, wanted, line, set())
+    return found
+
+
 def check_device_code():
-    """Raise if any source compiles to a reversed-operand DPP instruction."""
+    """Raise if any source compiles to a reversed-operand DPP instruction, or to a memory instruction too close behind
+    the vector instruction that writes its scalar registers."""
     sources = SOURCES + EXPERT_SOURCES
     with ThreadPoolExecutor(4) as pool:
         for src, text in zip(sources, pool.map(device_assembly, sources)):
             bad = sorted(set(m.group(0) for m in REVERSED_DPP.finditer(text)))
             if bad:
                 raise RuntimeError("%s: generated code holds %s" % (os.path.basename(src), ", ".join(bad)))
+            for write, read in early_scalar_reads(text):
+                raise RuntimeError("%s: fewer than %d wait states between '%s' and '%s'"
+                                   % (os.path.basename(src), SCALAR_WAIT_STATES, write, read))
 
 
 def _link(library, sources, verbose):

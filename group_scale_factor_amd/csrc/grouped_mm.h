@@ -405,7 +405,7 @@ __device__ __forceinline__ void load_to_lds(const v4u &rsrc, uint32_t lds, uint3
         "buffer_load_dwordx4 %1, %2, %3 offen lds"
         :
         : "s"(lds), "v"(off), "s"(rsrc), "s"(skip)
-        : "memory");
+        : "m0", "memory");
   else
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -413,7 +413,7 @@ __device__ __forceinline__ void load_to_lds(const v4u &rsrc, uint32_t lds, uint3
         "buffer_load_dword %1, %2, %3 offen lds"
         :
         : "s"(lds), "v"(off), "s"(rsrc), "s"(skip)
-        : "memory");
+        : "m0", "memory");
 }
 
 // All but the newest LEFT loads of this wave are complete.

@@ -97,3 +97,33 @@ def test_token_moves_read_slots_from_lanes_that_are_there():
     for name, lines in found.items():
         reads, narrowed = narrowed_lane_reads(lines)
         assert reads and not narrowed, name
+
+
+def test_the_build_check_finds_early_scalar_reads():
+    """By hand: the pair, what stands between it, and whether it is too close. Also over a branch."""
+    load = "buffer_load_dwordx4 v1, s[8:11], s40 offen lds"
+    m0 = "s_mov_b32 m0, s3\ns_nop 0\n"
+    for between, close in [("", True), (m0, True), (m0 + "v_mov_b32_e32 v9, 0\ns_add_i32 s3, s3, 1\n", True),
+                           (m0 + "s_nop 2\n", False), ("s_nop 3\n", True), ("s_nop 4\n", False)]:
+        for write, read in [("v_readfirstlane_b32 s9, v3", True), ("v_readlane_b32 s40, v250, 3", True),
+                            ("v_cmp_eq_u32_e64 s[10:11], v0, v1", True), ("v_readfirstlane_b32 s12, v3", False),
+                            ("s_mov_b32 s9, s4", False)]:
+            text = "_Zk:  ; @_Zk\n%s\n%s;;#ASMSTART\n%s\n;;#ASMEND\ns_endpgm\n.Lfunc_end0:\n" % (write, between, load)
+            found = _build.early_scalar_reads(text)
+            assert found == ([(write, load)] if close and read else []), (between, write)
+    loop = ("_Zk:\ns_nop 7\n.LBB0_1:\n%s\n%s\nv_readlane_b32 s40, v2, 1\ns_cbranch_scc1 .LBB0_1\ns_endpgm\n"
+            ".Lfunc_end0:\n")
+    assert len(_build.early_scalar_reads(loop % ("s_nop 1", load))) == 1
+    assert _build.early_scalar_reads(loop % ("s_nop 3", load)) == []
+
+
+@pytest.mark.parametrize("kind", ["mx", "fp8"])
+def test_loads_to_lds_say_that_they_write_m0(assembly, kind):
+    """Nothing that the compiler makes itself may rely on m0 around them."""
+    lines = [line for found in (kernels(assembly[kind], n) for n in ("mm_tile_kernel", "mm_paired_kernel"))
+             for lines in found.values() for line in lines]
+    writes = [line for line in lines if re.match(r"s_mov_b32 m0, s\d+$", line)]
+    assert len(writes) == sum("offen lds" in line for line in lines) > 0
+    assert len([line for line in lines if re.search(r"\bm0\b", line)]) == len(writes)
+    source = open(PRODUCTS["mx"].rsplit("/", 1)[0] + "/grouped_mm.h").read()
+    assert source.count("offen lds") == source.count(': "m0", "memory");')
