@@ -416,11 +416,12 @@ __device__ __forceinline__ void load_to_lds(const v4u &rsrc, uint32_t lds, uint3
         : "m0", "memory");
 }
 
-// All but the newest LEFT loads of this wave are complete.
-template <int LEFT>
+// All but the newest LEFT loads of this wave are complete; with READS its reads of LDS, too: a barrier behind which
+// others write there stands behind them by itself, not by where the compiler puts the products that use them.
+template <int LEFT, bool READS = false>
 __device__ __forceinline__ void wait_loads() {
   static_assert(LEFT < 64, "six bits of the count: 0..3 and 14, 15");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (LEFT & 15) | (LEFT >> 4 << 14));
+  __builtin_amdgcn_s_waitcnt((READS ? 0x0070 : 0x0f70) | (LEFT & 15) | (LEFT >> 4 << 14));
 }
 
 __device__ __forceinline__ v4u raw_buffer(const void *base, uint32_t bytes) {
@@ -653,12 +654,12 @@ __global__ __launch_bounds__(TW *NW *kWave) void mm_tile_kernel(MmParams p) {
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) stage(s);
     for (int s = 0; s < steps; ++s) {
-      wait_loads<(STAGES - 2) * S::Loads>();      // this wave's part of stage s is in LDS
-      __builtin_amdgcn_s_barrier();               // and everyone's; nobody reads the stage before it any more
+      wait_loads<(STAGES - 2) * S::Loads, true>();      // this wave's part of stage s is in LDS
+      __builtin_amdgcn_s_barrier();                     // and everyone's; nobody reads the stage before it any more
       stage(s + STAGES - 1);
       multiply(s);
     }
-    wait_loads<0>();                              // the out-of-range ones too
+    wait_loads<0, true>();                        // the out-of-range ones too
     __builtin_amdgcn_s_barrier();                 // nothing is under way into LDS, and nobody reads it any more
     // the products have to be done by the whole wave, before the branches of the stores below
 #pragma unroll

@@ -127,3 +127,18 @@ def test_loads_to_lds_say_that_they_write_m0(assembly, kind):
     assert len([line for line in lines if re.search(r"\bm0\b", line)]) == len(writes)
     source = open(PRODUCTS["mx"].rsplit("/", 1)[0] + "/grouped_mm.h").read()
     assert source.count("offen lds") == source.count(': "m0", "memory");')
+
+
+@pytest.mark.parametrize("kind", ["mx", "fp8"])
+def test_barriers_of_staged_tiles_wait_for_the_reads_before_them(assembly, kind):
+    """Behind a barrier the next loads write where the wave has just read: its reads are waited for at the barrier
+    itself, and on every way to it in the tiles of paired waves, which wait in the slot."""
+    for name, lines in kernels(assembly[kind], "mm_tile_kernel").items():
+        before = [lines[i - 1] for i, line in enumerate(lines) if line == "s_barrier"]
+        assert len(before) == 2, name
+        assert all(line.startswith("s_waitcnt vmcnt(") and "lgkmcnt(0)" in line for line in before), (name, before)
+    for name, lines in kernels(assembly[kind], "mm_paired_kernel").items():
+        reading = False
+        for line in lines:
+            reading = (reading or line.startswith("ds_read")) and not re.match(r"s_waitcnt .*lgkmcnt\(0\)", line)
+            assert line != "s_barrier" or not reading, name
