@@ -43,6 +43,9 @@ constexpr int kStep = 128;                    // bytes of k per matrix instructi
 constexpr int kTileBytes = 512;               // one 128 x 4 tile of blocked scales
 constexpr uint32_t kAnyBytes = 0x80000000u;   // buffer size above every valid offset, below kOutOfRange
 constexpr int kUnitScales = 0x7f7f7f7f;       // E8M0 2^0 in every byte
+// Both scales the constant 0: the builtin is the instruction without scales, which takes no register for them. (As a
+// scale, byte 0 would be 2^-127: a test reads off the assembly that no product is made with one.)
+constexpr int kNoScales = 0;
 
 struct MmParams {
   const uint8_t *a, *b;       // codes: t and w of every job
@@ -935,7 +938,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int at = i * 4 + n;
-        part[at % (kBehind + 1)] = mfma(w[n], t[i & 3], v4f{0, 0, 0, 0}, 0, 0);
+        part[at % (kBehind + 1)] = mfma(w[n], t[i & 3], v4f{0, 0, 0, 0}, kNoScales, kNoScales);
         if (at >= kBehind) add(at - kBehind);
         __builtin_amdgcn_sched_barrier(0);
       }

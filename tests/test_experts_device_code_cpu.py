@@ -142,3 +142,18 @@ def test_barriers_of_staged_tiles_wait_for_the_reads_before_them(assembly, kind)
         for line in lines:
             reading = (reading or line.startswith("ds_read")) and not re.match(r"s_waitcnt .*lgkmcnt\(0\)", line)
             assert line != "s_barrier" or not reading, name
+
+
+def test_products_of_any_scales_take_the_instruction_without_scales(assembly):
+    """Paired waves that multiply the sums by block-128 scales give the products none: every product of the row groups,
+    and those that start from nothing of the token groups, whose others add to a total and take the scales."""
+    for name, lines in kernels(assembly["fp8"], "mm_paired_kernel").items():
+        products = [line for line in lines if "mfma" in line]
+        plain = [line for line in products if line.startswith("v_mfma_f32_16x16x128_f8f6f4 ")]
+        scaled = [line for line in products if line.startswith("v_mfma_scale_f32_16x16x128_f8f6f4 ")]
+        assert len(plain) + len(scaled) == len(products) and plain, name
+        assert all(re.search(r"\], 0$", line) for line in plain), name
+        if "ILb0ELb0E" in name:
+            assert not scaled, name
+        else:
+            assert scaled and not any(re.search(r"\], 0, ", line) for line in scaled), name
