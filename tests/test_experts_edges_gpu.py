@@ -1,11 +1,11 @@
-"""Calls at the edges of the expert layer's operators: what no group or row of them may notice (GPU)."""
+"""Calls at the edges of the expert layer's operators (GPU): no tokens, no depth, groups of no tokens among others,
+scales of another kind. Products are held to the bounds that test_experts_products_gpu.py derives."""
 
-import numpy as np
 import pytest
 import torch
 
 import group_scale_factor_amd as gsf
-from test_experts_products_gpu import DEV, ends_of, random_codes
+from test_experts_products_gpu import DEV, ends_of, fp8_dequant, k_reference, near, random_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,31 @@ def test_row_products_over_no_depth_are_zeros(kind, sizes, tail, N):
     mm = gsf.mx_grouped_mm_M_groups if kind == "mx" else gsf.fp8_grouped_mm_M_groups
     assert mm(a, asc, w, wsc, ends_of(sizes), out=out) is out
     assert bool((out == 0).all())
+
+
+# Block-128 scales that are no powers of two among large tiles of token groups, whose workgroups change over to
+# multiplications there: (step of 36, row, value) at the first, a middle and the last step of a tile and of a workgroup,
+# in the first and the last row, next to a tile's edge, in several; a zero, a negative, a subnormal and a huge number.
+TOKEN_OTHERS = [[(35, 0, 1.5)], [(35, -1, 0.75)], [(3, 255, 2.0 ** -130), (4, 256, 1e30)], [(4, 0, -2.0)], [(9, 511, 0.0)],
+                [(17, -1, 3.0), (18, 0, 3.0)], [(0, -1, 0.7), (11, 3, 1e-3), (34, 257, -5.0)],
+                [(b, 7 * b, 0.7) for b in range(36)]]
+
+
+@pytest.mark.parametrize("others", TOKEN_OTHERS)
+@pytest.mark.parametrize("side", [0, 1])
+def test_other_scales_among_large_token_tiles(others, side):
+    sizes, M, N = [500, 0, 700, 1, 128] * 3, 1272, 1528
+    padded = [-(-n // 128) * 128 for n in sizes]
+    ends, T = ends_of(sizes), sum(sizes)
+    Tp = gsf.fp8_quantize_cols_K_groups_tokens(T, len(sizes))
+    gen = torch.Generator(device=DEV).manual_seed(100 + side)
+    codes = [random_codes(gen, n, Tp, narrow=True) for n in (M, N)]
+    scales = [torch.exp2(torch.randint(-12, 12, (Tp // 128, n), generator=gen, device=DEV).double()).float()
+              for n in (M, N)]
+    for step, row, value in others:
+        scales[side][step, row] = value
+    got = gsf.fp8_grouped_mm_K_groups(codes[0], scales[0], codes[1], scales[1], ends)
+    near(got, *k_reference(fp8_dequant(codes[0], scales[0].t()), fp8_dequant(codes[1], scales[1].t()), padded),
+         max(padded), narrow=True)
+    again = gsf.fp8_grouped_mm_K_groups(codes[0], scales[0], codes[1], scales[1], ends)
+    assert torch.equal(got, again)
