@@ -60,7 +60,7 @@ for t in (bf16, f16, f32):
                                                                              dweights=o[1]), ((T * k, D), t), ((T, k), f32))
 
 # products of row groups: streamed, 32 x 128, 128 x 128 and 256 x 256 tiles
-for sizes, K, N in (([1], 128, 16), ([1, 2, 1, 0, 4], 1408, 4096), ([300, 0, 77, 1, 513], 1376, 1003),
+for sizes, K, N in (([1], 128, 16), ([1, 2, 1, 0, 4], 1408, 4096), ([1300, 0, 777, 1, 923], 1376, 1003),
                     ([5000, 7001], 256, 2056)):
     rows = sum(sizes)
     a, asc, w, wsc, ends = mx_m_inputs(sizes, 0, K, N, 1)
@@ -71,7 +71,7 @@ for sizes, K, N in (([1], 128, 16), ([1, 2, 1, 0, 4], 1408, 4096), ([300, 0, 77,
         ((rows, N), bf16))
 
 # products of token groups; the casts
-for sizes, M, N in (([32], 16, 16), ([640, 0, 2080], 40, 600), ([640, 0, 2080], 512, 1003),
+for sizes, M, N in (([32], 16, 16), ([640, 0, 2080], 40, 4000), ([640, 0, 2080], 1408, 1003),
                     ([512, 0, 704, 32, 128] * 3, 1272, 1528)):
     T, G, ends = sum(sizes), len(sizes), ends_of(sizes)
     a, b = random_codes(gen, M, T), random_codes(gen, N, T)
