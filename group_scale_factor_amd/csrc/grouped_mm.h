@@ -699,7 +699,7 @@ __global__ __launch_bounds__(TW *NW *kWave) void mm_tile_kernel(MmParams p) {
 // for its first loads (2000 to 5000 cycles from nothing) and to store its outputs (3000) then overlaps with steps,
 // which take 3000 cycles each. Against a workgroup for each tile: K groups of 8 steps (16 groups, outputs of 8192 x
 // 5120) 852 -> 798 us; row groups of 11 steps (131072 rows, N 5120) 1055 -> 995; of 40 steps the same. From there on
-// the card's power sets the rate: 8192 x 8192 x 8192 takes 410 to 440 us on different cards (2.5 to 2.7 PFLOP/s at
+// the card's power sets the rate: 8192 x 8192 x 8192 takes 384 to 440 us on different cards (2.5 to 2.9 PFLOP/s at
 // 1.65 to 1.9 GHz).
 //
 // Block-128 scales multiply a product's sums, and over k that is a multiplication and an addition for each of them
@@ -708,7 +708,7 @@ __global__ __launch_bounds__(TW *NW *kWave) void mm_tile_kernel(MmParams p) {
 // by 2^(byte - 127) anyway: the exponent is the byte. A workgroup takes that for granted, and each wave looks at 64 of
 // a step's 512 scales; the first other one ends it, and the workgroup does the tile again, and the ones after it, with
 // the multiplications. (Both kinds in one loop write the sums from two places, and 500 registers spill.) Seven groups
-// of 32001 tokens, 1408 x 7168: 385 -> 350 us; with any scales 8192 x 8192 x 8192 takes 561 us for 555. Row groups
+// of 32001 tokens, 1408 x 7168: 385 -> 350 us, now 340 to 363; with any scales 8192 x 8192 x 8192 takes 561 us for 555. Row groups
 // keep the multiplications: there they are half as many (a step has one scale of w), and weights often have any scales.
 
 template <bool MX, bool DEPTH>

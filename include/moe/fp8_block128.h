@@ -112,7 +112,7 @@ int fp8_grouped_mm_M_groups(const uint8_t *a, const float *a_scales, int64_t row
  *
  * a, b      device codes, M x Tp and N x Tp, dense, 16-byte aligned (fp8_quantize_cols_K_groups' qT for the
  *           same offsets); Tp = round_up(T, 128) + 128*num_groups. Offsets are clamped into [previous end,
-           Tp - 128*num_groups].
+ *           Tp - 128*num_groups].
  * a_scales, b_scales  device float, (Tp/128) x M and (Tp/128) x N.
  * out       device bf16, num_groups x M x N, dense.
  * 1 <= num_groups <= 2048; Tp <= 2^22; M, N < 2^24. One kernel on `stream`.
