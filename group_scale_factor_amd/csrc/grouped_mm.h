@@ -65,7 +65,8 @@ struct MmParams {
   int m_tiles;                // depth: M tiles
 };
 
-// One output tile. Everything is the same for the whole workgroup.
+// One output tile. Everything is the same for the whole workgroup. What K = 0 leaves alone stays as it was, so a Job
+// starts as zeros: the paired kernel issues the loads of such a tile, too, out of range of buffers that are none.
 struct Job {
   const uint8_t *t, *w;       // first row of the tile, first k
   int t_rows, w_rows;         // valid rows from there
@@ -750,7 +751,7 @@ __global__ __launch_bounds__(512) void mm_paired_kernel(MmParams p) {
       }
     return false;
   };
-  Job j;      // the tile whose steps are loaded
+  Job j = {};      // the tile whose steps are loaded
   if (!find(p.offs, j)) return;
   int32_t *ends = reinterpret_cast<int32_t *>(mm_lds + kEnds);
   if (wave == 0 && p.groups <= kWave && lane < p.groups) ends[lane] = p.offs[lane];

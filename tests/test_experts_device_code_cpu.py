@@ -157,3 +157,61 @@ def test_products_of_any_scales_take_the_instruction_without_scales(assembly):
             assert not scaled, name
         else:
             assert scaled and not any(re.search(r"\], 0, ", line) for line in scaled), name
+
+
+def registers(operand):
+    """Scalar registers of an operand, by number."""
+    m = re.match(r"s(\d+)$|s\[(\d+):(\d+)\]$", operand)
+    if not m:
+        return []
+    return [int(m.group(1))] if m.group(1) else list(range(int(m.group(2)), int(m.group(3)) + 1))
+
+
+def loads_from_unset_buffers(lines, given):
+    """Loads to LDS before the first barrier whose buffer, or whose step of it, may lie in scalar registers that nothing
+    on the way has set; the first `given` are set at the start. A copy of an unset register is unset, too."""
+    at = {line.split(":")[0]: i for i, line in enumerate(lines) if line.startswith(".LBB")}
+    unset = [None] * len(lines)
+    work = [(0, frozenset(range(given, 106)))]
+    found = set()
+    while work:
+        i, state = work.pop()
+        while i < len(lines):
+            if unset[i] is not None and state <= unset[i]:
+                break
+            state = unset[i] = state | (unset[i] or frozenset())
+            line = lines[i]
+            name, _, rest = line.partition(" ")
+            ops = [op.strip() for op in rest.split(",")]
+            if "offen lds" in line:
+                used = registers(ops[1]) + registers(ops[2].split()[0])
+                found.update((i, r) for r in used if r in state)
+            elif name.startswith(("s_mov_b", "s_and_b")) and len(registers(ops[0])) > 0:
+                to = registers(ops[0])
+                froms = [registers(op) for op in ops[1:]]
+                for n, r in enumerate(to):
+                    bad = any(n < len(f) and f[n] in state for f in froms)
+                    state = state | {r} if bad else state - {r}
+            elif name.startswith(("s_", "v_")) and not name.startswith(("s_cmp", "s_cbranch", "s_branch", "s_bitcmp")):
+                state = state - set(registers(ops[0]))
+                if name.startswith("v_") and len(ops) > 1:      # a carry or a condition beside the vector result
+                    state = state - set(registers(ops[1]) if "_co_" in name else [])
+            m = re.match(r"s_(c?branch\S*) (\.LBB\S+)", line)
+            if m:
+                work.append((at[m.group(2)], state))
+            if line.startswith(("s_branch", "s_endpgm")):
+                break
+            i += 1
+    first = lines.index("s_barrier")
+    return sorted({(lines[i], r) for i, r in found if i < first})
+
+
+@pytest.mark.parametrize("kind", ["mx", "fp8"])
+def test_no_first_load_goes_by_a_buffer_that_was_not_set(assembly, kind):
+    """A tile with nothing to load (rows in no group) issues its loads all the same, out of range of its buffers: their
+    sizes have to be set for it, too, where it is the first one of its workgroup. (Later tiles find the last one's.)"""
+    text = assembly[kind]
+    for name, lines in kernels(text, "mm_paired_kernel").items():
+        block = text[text.index(".amdhsa_kernel " + name):]
+        given = int(re.search(r"\.amdhsa_user_sgpr_count (\d+)", block).group(1)) + 1     # and the workgroup's number
+        assert loads_from_unset_buffers(lines, given) == [], name

@@ -1,11 +1,13 @@
 """Calls at the edges of the expert layer's operators (GPU): no tokens, no depth, groups of no tokens among others,
-scales of another kind. Products are held to the bounds that test_experts_products_gpu.py derives."""
+scales of another kind, workgroups that start with rows in no group. Products are held to the bounds that
+test_experts_products_gpu.py derives."""
 
 import pytest
 import torch
 
 import group_scale_factor_amd as gsf
-from test_experts_products_gpu import DEV, ends_of, fp8_dequant, k_reference, near, random_codes
+from test_experts_products_gpu import (DEV, ends_of, fp8_dequant, fp8_m_inputs, k_reference, m_reference, mx_dequant,
+                                       mx_m_inputs, near, random_codes)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +89,23 @@ def test_other_scales_among_large_token_tiles(others, side):
          max(padded), narrow=True)
     again = gsf.fp8_grouped_mm_K_groups(codes[0], scales[0], codes[1], scales[1], ends)
     assert torch.equal(got, again)
+
+
+# Large tiles whose workgroups start with rows in no group: fewer tiles than compute units, and no rows in groups at all
+@pytest.mark.parametrize("sizes,tail,K,N", [([584] * 16, 896, 2048, 1024), ([0] * 16, 10240, 256, 1024),
+                                            ([0, 2600, 0], 7000, 384, 1500)])
+@pytest.mark.parametrize("kind", ["mx", "fp8"])
+def test_workgroups_that_start_with_rows_in_no_group(kind, sizes, tail, K, N):
+    make = mx_m_inputs if kind == "mx" else fp8_m_inputs
+    a, asc, w, wsc, ends = make(sizes, tail, K, N, K + N, narrow=True)
+    rows = a.shape[0]
+    out = torch.full((rows, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    if kind == "mx":
+        av, wv = mx_dequant(a, asc), lambda e: mx_dequant(w[e], wsc[e])
+        gsf.mx_grouped_mm_M_groups(a, gsf.mx_block_rearrange_M_groups(asc, ends), w, gsf.mx_block_rearrange_3d(wsc), ends,
+                                   out=out)
+    else:
+        av, wv = fp8_dequant(a, asc.t()), lambda e: fp8_dequant(w[e], wsc[e].repeat_interleave(128, 0)[:N])
+        gsf.fp8_grouped_mm_M_groups(a, asc, w, wsc, ends, out=out)
+    near(out, *m_reference(av, wv, sizes, rows, N), K, narrow=True)
+    assert bool((out[rows - tail:] == 0).all())
