@@ -399,7 +399,10 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 // not see this load: it orders nothing after it and waits for it nowhere, so a product may read one stage while the
 // other fills; wait_loads() before the barrier is what completes it. Lanes out of range write zeros.
 // `skip` (uniform) is added to every lane's offset; the range check counts it (measured: zeros from the buffer's end
-// on for offset + skip, also where offset + skip passes 2^32).
+// on for offset + skip, also where offset + skip passes 2^32 or skip alone the size). m0 is declared as written: the
+// compiler reserves it, warns of that, and makes it anew wherever it needs it itself (which is nowhere here).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(const v4u &rsrc, uint32_t lds, uint32_t off, uint32_t skip = 0) {
   if (BYTES == 16)
@@ -419,6 +422,7 @@ __device__ __forceinline__ void load_to_lds(const v4u &rsrc, uint32_t lds, uint3
         : "s"(lds), "v"(off), "s"(rsrc), "s"(skip)
         : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // All but the newest LEFT loads of this wave are complete; with READS its reads of LDS, too: a barrier behind which
 // others write there stands behind them by itself, not by where the compiler puts the products that use them.
